@@ -159,6 +159,13 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The larger of two, NaN if either is (fmaxf takes the other one then).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // Store kVecs 16-byte pieces of each lane's row (row: its address, null for a row that is not
 // stored; pieces at or past `vecs` are not either). Four lanes trade pieces first, so that each
 // store covers 64 contiguous bytes of eight rows: a lane storing its own row piece by piece
@@ -201,12 +208,13 @@ __device__ __forceinline__ void store_rows(uint16_t* row, uint4 (&v)[kVecs], int
 // 2^a and 2^b without the special-function unit, whose 16 results a cycle would bound the softmax:
 // x = n + f with n the nearest whole number (the addition of 1.5 * 2^23 leaves it in the low
 // bits), 2^f by a polynomial of degree 4 interpolated at Chebyshev nodes on [-1/2, 1/2] (relative
-// error 3.7e-6, a thousandth of the bf16 step the result is rounded to), and n added to the
-// exponent. Below -126 the result is 2^-126.
+// error 3.7e-6, a thousandth of the bf16 step the result is rounded to), times 2^n, whose bits are
+// n's moved into the exponent. Below -126 the result is 2^-126. NaN stays NaN: the maximum keeps it
+// and so does the product (n added to 2^f's own exponent bits would make a number of it).
 __device__ __forceinline__ void ex2_poly(uint64_t x, float& a, float& b) {
   float x0, x1;
   unpair_f32(x, x0, x1);
-  x = pair_f32(fmaxf(x0, -126.0f), fmaxf(x1, -126.0f));
+  x = pair_f32(max_nan(x0, -126.0f), max_nan(x1, -126.0f));
   const uint64_t big = pair_f32(12582912.0f, 12582912.0f), unbig = pair_f32(-12582912.0f, -12582912.0f);
   const uint64_t minus = pair_f32(-1.0f, -1.0f);
   const uint64_t r = add_f32x2(x, big);
@@ -216,11 +224,11 @@ __device__ __forceinline__ void ex2_poly(uint64_t x, float& a, float& b) {
   y = fma_f32x2(y, f, pair_f32(0.2402210682630539f, 0.2402210682630539f));
   y = fma_f32x2(y, f, pair_f32(0.6931210160255432f, 0.6931210160255432f));
   y = fma_f32x2(y, f, pair_f32(1.0000001192092896f, 1.0000001192092896f));
-  float y0, y1, r0, r1;
-  unpair_f32(y, y0, y1);
+  float r0, r1;
   unpair_f32(r, r0, r1);
-  a = __uint_as_float((__float_as_uint(r0) << 23) + __float_as_uint(y0));
-  b = __uint_as_float((__float_as_uint(r1) << 23) + __float_as_uint(y1));
+  constexpr uint32_t kOne = 0x3F800000u;
+  unpair_f32(mul_f32x2(y, pair_f32(__uint_as_float((__float_as_uint(r0) << 23) + kOne),
+                                   __uint_as_float((__float_as_uint(r1) << 23) + kOne))), a, b);
 }
 
 // A ring's place and phase, moved on by `by` of `size` entries.

@@ -531,3 +531,28 @@ def test_many_rows_do_not_hide_what_is_not_a_number_and_grow():
 def test_many_tiles_backward(hq, hkv, d, causal, window):
     # several tiles of each kernel for every block, empty ones among them
     check(Problem([300, 1, 700, 129, 0, 513], [300, 64, 650, 400, 9, 513], hq, hkv, d, causal, window, seed=d + window))
+
+
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("causal", [False, True])
+def test_backward_does_not_hide_what_is_not_a_number(d, causal):
+    # one query at a time, at neighbouring places of a step, has a lse (then a Q) that is not a number: nothing that its
+    # probabilities enter is a plausible number, and no other head or key notices
+    n = 40
+    for i in (0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 31, 32, 39):
+        p = Problem([n], [n], 2, 2, d, causal, seed=7)
+        O, lse = p.forward()
+        lse[i, 1] = float("nan")
+        dQ, dK, dV = p.backward(O, lse)
+        seen = i + 1 if causal else n
+        assert dQ[i, 1].isnan().all(), i
+        for name, t in (("dK", dK), ("dV", dV)):
+            assert t[:seen, 1].isnan().all(), (name, i)
+            assert t[seen:, 1].isfinite().all() and t[:, 0].isfinite().all(), (name, i)
+        rest = [j for j in range(n) if j != i]
+        assert dQ[rest, 1].isfinite().all() and dQ[:, 0].isfinite().all()
+    p = Problem([n], [n], 2, 2, d, causal, seed=7)
+    p.Q[8, 0] = float("nan")
+    dQ, dK, dV = p.backward(*p.forward())
+    for t in (dQ[8:9], dK[:9 if causal else n], dV[:9 if causal else n]):
+        assert t[:, 0].isnan().all() and t[:, 1].isfinite().all()
