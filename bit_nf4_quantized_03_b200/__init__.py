@@ -498,7 +498,12 @@ def _workspace(ws, need: int, like: torch.Tensor, stream):
         if stream is None:
             ws = torch.empty(need, dtype=torch.uint8, device=like.device)
         else:
-            s = torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream
+            if not isinstance(stream, int):
+                s = stream
+            elif stream == 0:        # ExternalStream(0) is not the default stream but a new one
+                s = torch.cuda.default_stream(like.device)
+            else:
+                s = torch.cuda.ExternalStream(stream, device=like.device)
             with torch.cuda.stream(s):
                 ws = torch.empty(need, dtype=torch.uint8, device=like.device)
     if ws is not None and not ws.is_contiguous():

@@ -203,6 +203,35 @@ def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
         q._device(_Fake(0), _Fake(-1))               # a CPU tensor
 
 
+def test_a_workspace_is_allocated_on_the_stream_of_its_call(monkeypatch):
+    # memory from another stream's pool could be handed out again there while the call still runs
+    now, seen = ["current"], []
+
+    class On:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.s
+
+        def __exit__(self, *exc):
+            now[0] = self.before
+
+    empty = torch.empty
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    # as torch has it: address 0 is no stream of anybody's, so a new one is made
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda at, device=None: f"external {at}" if at else "new")
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: (seen.append(now[0]), empty(*a, **k))[1])
+    like = torch.zeros(1)
+    for stream in (None, 0, 77, "side"):
+        ws, n = q._workspace(None, 64, like, stream)
+        assert n == 64 and ws.numel() == 64
+    assert seen == ["current", "default", "external 77", "side"]
+    assert q._workspace(None, 0, like, 0) == (None, 0) and q._workspace(ws, 64, like, 0)[0] is ws
+    assert len(seen) == 4
+
+
 # --------------------------------------------------------------- attention --
 def _attn(**kw):
     a = dict(batch=2, heads_q=4, heads_kv=2, head_dim=64, causal=1, window=0, scale=0.125, reserved=0, tokens_q=8,

@@ -231,3 +231,28 @@ def test_generation_step_continues_a_prefill():
     torch.cuda.synchronize()
     assert torch.equal(r, r2) and torch.equal(h, h2)
     q.qlora_check_device_error()
+
+
+def test_workspaces_belong_to_the_stream_of_their_call(monkeypatch):
+    # the calls that allocate one, on the default stream by its address, on a side stream by its address and as an object
+    side = torch.cuda.Stream()
+    x = torch.randn(40, 2, 64, device="cuda").to(BF)
+    lse = torch.zeros(40, 2, device="cuda")
+    keys = torch.randn(3000, 2, 64, device="cuda").to(BF)
+    g = [torch.empty_like(x) for _ in range(3)]
+    rows, w = torch.randn(40, 128, device="cuda").to(BF), torch.ones(128, device="cuda")
+    O, dx, dw = torch.empty_like(x), torch.empty_like(rows), torch.empty_like(w)
+    O1 = torch.empty_like(x[:1])
+    seen, empty = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: (seen.append(torch.cuda.current_stream().cuda_stream), empty(*a, **k))[1])
+    for stream, at in ((None, 0), (0, 0), (torch.cuda.default_stream(), 0), (side.cuda_stream, side.cuda_stream),
+                       (side, side.cuda_stream)):
+        side.wait_stream(torch.cuda.current_stream())
+        seen.clear()
+        q.qlora_attention_fwd(x, x, x, O, lse, causal=True, stream=stream)
+        q.qlora_attention_bwd(x, x, x, O, x, lse, *g, causal=True, stream=stream)
+        q.qlora_attention_fwd(x[:1], keys, keys, O1, stream=stream)
+        q.qlora_norm_residual_bwd(None, rows, rows, None, None, None, w, dx, dw_pre=dw, stream=stream)
+        assert seen == [at] * 3, stream
+        torch.cuda.synchronize()
+    q.qlora_check_device_error()
