@@ -297,12 +297,10 @@ def qlora_nf4_quantize_workspace_bytes(n: int, k: int, mode: int) -> int:
 
 
 def qlora_nf4_quantize(W: torch.Tensor, w: QuantizedWeight, ws: torch.Tensor | None = None, stream=None):
-    """Quantize fp32 W [n, k] into w (allocates a workspace tensor if none is given)."""
-    need = qlora_nf4_quantize_workspace_bytes(w.n, w.k, w.mode)
-    if ws is None and need > 0:
-        ws = torch.empty(need, dtype=torch.uint8, device=W.device)
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(lib().qlora_nf4_quantize(_ptr(W), w.ref(), _ptr(ws), ws_bytes, _stream(stream)), "qlora_nf4_quantize")
+    """Quantize fp32 W [n, k] into w (allocates a workspace tensor on the call's stream if none is given)."""
+    at = _ptr(W)
+    ws, ws_bytes = _workspace(ws, qlora_nf4_quantize_workspace_bytes(w.n, w.k, w.mode), W, stream)
+    _check(lib().qlora_nf4_quantize(at, w.ref(), _ptr(ws), ws_bytes, _stream(stream)), "qlora_nf4_quantize")
     return w
 
 

@@ -102,3 +102,20 @@ def test_double_quant_65b_gate_shape_full():
     for r_ in rows:
         want = o.pack_nibbles(o.nf4_codes(W[r_].numpy()))
         assert np.array_equal(codes[r_], want)
+
+
+def test_quantize_on_another_stream_has_its_workspace_there(monkeypatch):
+    W = synth.weight(300, 256)
+    want = gpu_weight_dict(gpu_quantize(W, q.QLORA_SCALE_DQ_FP8))
+    Wd, side = W.cuda(), torch.cuda.Stream()
+    qw = q.QuantizedWeight(300, 256, q.QLORA_SCALE_DQ_FP8)
+    seen, empty = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: (seen.append(torch.cuda.current_stream().cuda_stream), empty(*a, **k))[1])
+    for stream, at in ((None, 0), (0, 0), (side, side.cuda_stream), (side.cuda_stream, side.cuda_stream)):
+        side.wait_stream(torch.cuda.current_stream())
+        seen.clear()
+        q.qlora_nf4_quantize(Wd, qw, stream=stream)
+        assert seen == [at], stream
+        torch.cuda.synchronize()
+        assert_weight_bitexact(gpu_weight_dict(qw), want)
+    q.qlora_check_device_error()
