@@ -165,6 +165,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (warp == kMathWarps + 3) {
     // ------------------------------------------------------------ scheduler
     const int64_t items = static_cast<int64_t>(p.tiles) * p.heads_kv;
+    // Tiles there are at most, and exactly once a search has gone past the last one. Later items there are passed over
+    // without another search: with tens of thousands of sequences one takes half a millisecond, and the others, whose
+    // wait for a tile has a limit, gave up behind thousands of them.
+    int64_t tiles = p.tiles;
     RingPos at;
     int published = 0;
     bool ok = true;
@@ -181,7 +185,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         int64_t tile;
         int t = 0;
         decode_block(p, static_cast<uint32_t>(item), !kKeys && p.causal != 0, tile, w.head);
-        if (find_tile<kKeys>(p, per_res, tile, w.sq, t)) {      // there are a few items more than tiles
+        const int64_t which = tile;
+        if (which >= tiles) {
+          // there are a few items more than tiles
+        } else if (!find_tile<kKeys>(p, per_res, tile, w.sq, t)) {
+          tiles = which - tile;
+        } else {
           w.live = 1;
           w.ta = t * per_res;
           w.tokens = min(per_res, (kKeys ? w.sq.nk : w.sq.nq) - w.ta);

@@ -32,10 +32,10 @@ __device__ __forceinline__ void seq_range(const int32_t* cu, int64_t tokens, int
 }
 
 // Tile `idx` of the sequences' tiles in a row (`per` tokens each, of the keys or the queries):
-// its sequence and its place there; false past the last one. Whole warps call it; both
-// offset arrays are read in one round trip.
+// its sequence and its place there; false past the last one, and idx is then how far past. Whole
+// warps call it; both offset arrays are read in one round trip.
 template <bool kByKeys>
-__device__ __forceinline__ bool find_tile(const AttnParams& p, int per, int64_t idx, Seq& sq, int& t) {
+__device__ __forceinline__ bool find_tile(const AttnParams& p, int per, int64_t& idx, Seq& sq, int& t) {
   const int lane = threadIdx.x & 31;
   for (int base = 0; base < p.batch; base += 32) {
     int32_t q0 = 0, nq = 0, k0 = 0, nk = 0;

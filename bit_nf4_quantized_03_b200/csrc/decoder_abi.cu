@@ -221,7 +221,11 @@ static int attention_params(const qlora_attention* a, AttnParams* p) {
   // 32-bit token indexes in the kernels (elements have 64), with room for a tile and a window past the end; the
   // tensor maps hold strides below 2^40 bytes
   constexpr int64_t kMost = int64_t(1) << 30;
-  if (a->tokens_q > kMost || a->tokens_k > kMost || a->window > kMost || a->batch > kMost) return QLORA_ERR_UNSUPPORTED;
+  if (a->tokens_q > kMost || a->tokens_k > kMost || a->window > kMost) return QLORA_ERR_UNSUPPORTED;
+  // A warp walks over the sequences, 32 at a time or, past empty ones, one by one, at 0.7 us a round trip, while others
+  // wait for it, 2 s at most: a million one by one take 0.7 s.
+  constexpr int32_t kMostSequences = 1 << 20;
+  if (a->batch > kMostSequences) return QLORA_ERR_UNSUPPORTED;
   constexpr int64_t kMostLd = int64_t(1) << 38;
   if (a->ld_q > kMostLd || a->ld_k > kMostLd || a->ld_v > kMostLd || a->ld_o > kMostLd) return QLORA_ERR_UNSUPPORTED;
   const int64_t blocks = (std::max(a->tokens_q, a->tokens_k) + a->batch) * a->heads_kv * 16;

@@ -312,3 +312,12 @@ def test_attention_binding_refusals(L):
         q.qlora_attention_fwd(x.view(4, 128), x, x, x)
     with pytest.raises(ValueError):
         q.qlora_attention_bwd(x, x, x, x, x, None, x, x, x)
+
+
+def test_attention_takes_a_million_sequences(L):
+    # more are refused: some warps walk over them one by one while others wait, and that wait has a limit
+    many = dict(tokens_q=0, tokens_k=0, heads_q=1, heads_kv=1, ld_q=64, ld_k=64, ld_v=64, ld_o=64)
+    for batch, want in ((1 << 20, 0), ((1 << 20) + 1, 2)):
+        a = ctypes.byref(_attn(batch=batch, **many))
+        assert L.qlora_attention_fwd(a, None, None, None, None, None, None, 0, None) == want
+        assert L.qlora_attention_bwd(a, *[None] * 10, 0, None) == want

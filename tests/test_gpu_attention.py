@@ -556,3 +556,31 @@ def test_backward_does_not_hide_what_is_not_a_number(d, causal):
     dQ, dK, dV = p.backward(*p.forward())
     for t in (dQ[8:9], dK[:9 if causal else n], dV[:9 if causal else n]):
         assert t[:, 0].isnan().all() and t[:, 1].isfinite().all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_empty_sequences(causal):
+    # 200 samples among 40,000 sequences, nearly all of them empty: the grids' bounds count a tile more for each
+    n, each, hq, hkv, d = 40000, 100, 64, 64, 8
+    ends = torch.arange(0, n, n // 200)
+    lens = torch.zeros(n, dtype=torch.int64)
+    lens[ends] = each
+    cu = torch.zeros(n + 1, dtype=torch.int32)
+    cu[1:] = lens.cumsum(0)
+    p = Problem([each] * 200, [each] * 200, hq, hkv, d, causal, seed=14)
+    want = [*p.forward()]
+    want += p.backward(*want)
+    p.how = dict(p.how, cu_q=cu.cuda(), cu_k=cu.cuda())
+    got = p.backward(*want[:2])
+    assert all(torch.equal(a, b) for a, b in zip(want[2:], got))
+    # the forward's tiles follow the mean length here, so its steps may differ: one and the same bound holds
+    ref = p.forward()
+    assert float((ref[0].double() - want[0].double()).norm()) <= 2 * H * float(want[0].double().norm())
+    # and all of them behind the last sample, or before the first
+    for where in (slice(0, 200), slice(n - 200, n)):
+        lens.zero_()
+        lens[where] = each
+        cu[1:] = lens.cumsum(0)
+        p.how = dict(p.how, cu_q=cu.cuda(), cu_k=cu.cuda())
+        g = p.backward(*want[:2])
+        assert all(torch.equal(a, b) for a, b in zip(want[2:], g))
