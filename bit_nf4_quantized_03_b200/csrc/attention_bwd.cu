@@ -73,6 +73,22 @@ struct BwdWork {
   int32_t n;             // steps
 };
 
+// mbar_wait for the warp that hands out tiles, two ahead: the others may be at a tile of `steps` steps all the while. A
+// step takes about 2 us, so a tile of a million takes as long as any other wait may (2 s): 20 us a step on top.
+__device__ __forceinline__ bool wait_for_a_tile(uint64_t* bar, uint32_t parity, int steps) {
+  const uint32_t at = smem_u32(bar);
+  if (mbar_try_wait(at, parity)) return true;
+  const uint64_t t0 = globaltimer_ns(), limit = kWaitLimitNs + static_cast<uint64_t>(steps) * 20000u;
+  uint32_t tries = 0;
+  while (true) {
+    if (mbar_try_wait_suspend(at, parity, kSuspendHintNs)) return true;
+    if ((++tries & 15u) == 0 && globaltimer_ns() - t0 > limit) {
+      atomicCAS(&g_device_error, kErrNone, kErrWaitTimeout);
+      return false;
+    }
+  }
+}
+
 template <int kHD, bool kKeys>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_bwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnMaps maps) {
@@ -171,6 +187,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int64_t tiles = p.tiles;
     RingPos at;
     int published = 0;
+    int n[3] = {0, 0, 0};            // steps of the last three tiles handed out, the oldest first
     bool ok = true;
     // Tiles are handed out longest first, one counter for all blocks: which block sums a tile changes nothing in it.
     // (Dealt out beforehand, causal sequences left a sixth of the time to the unlucky blocks.)
@@ -206,15 +223,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
       }
       if (w.live == 0 && !last) continue;
-      if (published >= 2) ok = mbar_wait(&work_empty[at.at], at.phase ^ 1);
+      // the place is free once every role has taken n[1]'s tile, behind the end of n[0]'s
+      if (published >= 2) ok = wait_for_a_tile(&work_empty[at.at], at.phase ^ 1, n[0]);
       if (!ok) break;
       if (lane == 0) {
         work[at.at] = w;
         mbar_arrive(&work_full[at.at]);
       }
+      if (last) break;
       at.move(1, 2);
       ++published;
-      if (last) break;
+      n[0] = n[1];
+      n[1] = n[2];
+      n[2] = w.n;
     }
   } else if (warp == kMathWarps + 1) {
     // ------------------------------------------------------------ TMA producer

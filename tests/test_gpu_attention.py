@@ -584,3 +584,45 @@ def test_many_empty_sequences(causal):
         p.how = dict(p.how, cu_q=cu.cuda(), cu_k=cu.cuda())
         g = p.backward(*want[:2])
         assert all(torch.equal(a, b) for a, b in zip(want[2:], g))
+
+
+def test_a_tile_that_takes_seconds():
+    # backward: one sequence whose keys meet 290 million rows of queries (2.25 million steps of one tile), short ones behind
+    # it. The warp that hands out tiles is two ahead and has to wait for the long one's end. Queries are zero, so that the
+    # probabilities are 1 / keys, and only a few gradients are not.
+    nq, nk, more, heads, d = 4_500_000, 128, 600, 64, 8
+    tq, tk = nq + more, nk + more
+    g = torch.Generator(device="cuda")
+    g.manual_seed(15)
+    Q, O = (torch.zeros(tq, heads, d, dtype=BF, device="cuda") for _ in range(2))
+    K, V = (torch.randn(tk, 1, d, generator=g, device="cuda").to(BF) for _ in range(2))
+    lse = torch.zeros(tq, heads, device="cuda")
+    lse[:nq] = math.log(nk)
+    dO = torch.zeros_like(Q)
+    dO[nq - 3:] = torch.randn(more + 3, heads, d, generator=g, device="cuda").to(BF)
+    ends = torch.arange(more + 1, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    how = dict(cu_q=torch.cat((zero, nq + ends)), cu_k=torch.cat((zero, nk + ends)))
+    dK, dV = torch.full_like(K, 7.0), torch.full_like(V, 7.0)
+    dQ = torch.full_like(Q, 7.0)
+    q.qlora_attention_bwd(Q, K, V, O, dO, lse, dQ, dK, dV, **how)
+    q.qlora_check_device_error()
+    f = dO[nq - 3:].double()
+    # P is 1/128 and 1 up to the 32-bit exponential, its bf16 rounding exact: dV is a sum of dO's, rounded once
+    for at, of, n in ((slice(0, nk), f[:3].flatten(0, 1), nk), (slice(nk, tk), f[3:], 1)):
+        want = of.sum(0).expand(nk, d) / n if n > 1 else of.sum(1)
+        size = of.abs().sum(0).expand(nk, d) / n if n > 1 else of.abs().sum(1)
+        assert ((dV[at, 0].double() - want).abs() <= H * want.abs() + (H + F) * size).all()
+    assert (dK == 0).all()
+    # dS = P dO V^T with delta 0; dQ = scale dS K
+    for at, of, keys in ((slice(nq - 3, nq), f[:3], slice(0, nk)), (slice(nq, tq), f[3:], None)):
+        Kf, Vf = K[:, 0].double(), V[:, 0].double()
+        if keys is not None:
+            dS, E, Kk = of @ Vf[keys].T / nk, of.abs() @ Vf[keys].abs().T / nk, Kf[keys]
+            want, size = dS @ Kk, E @ Kk.abs()
+        else:
+            dS, E = (of * Vf[nk:, None]).sum(-1, keepdim=True), (of * Vf[nk:, None]).abs().sum(-1, keepdim=True)
+            want, size = dS * Kf[nk:, None], E * Kf[nk:, None].abs()
+        c = d ** -0.5
+        assert ((dQ[at].double() - c * want).abs() <= H * c * want.abs() + (H + F) * c * size).all()
+    assert not dQ[:nq - 3].any()
