@@ -293,6 +293,8 @@ int qlora_attention_bwd(const qlora_attention* a, const uint16_t* Q, const uint1
   AttnParams p;
   const int st = attention_params(a, &p);
   if (st != QLORA_OK) return st;
+  // the kernels count the query rows that a key head meets in 32 bits, with room for a tile of 64 heads a token
+  if (a->tokens_q * p.group > INT32_MAX - (128 << 6)) return QLORA_ERR_UNSUPPORTED;
   const bool q = a->tokens_q > 0, k = a->tokens_k > 0;
   if (!q && !k) return QLORA_OK;
   for (const void* t : {static_cast<const void*>(Q), static_cast<const void*>(O), static_cast<const void*>(dO),

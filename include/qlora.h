@@ -502,7 +502,8 @@ int qlora_norm_residual_bwd(const qlora_norm *n, const void *dr, const uint16_t 
  *    its results, whatever they are. Within a sequence inputs must be finite.
  * Limits: QLORA_ERR_UNSUPPORTED for head_dim, group or strides outside the above,
  * more than 2^20 sequences, or more than 2^30 tokens or tiles than one launch
- * holds: (max(tokens_q, tokens_k) + batch) * heads_kv is below 2^27.
+ * holds: (max(tokens_q, tokens_k) + batch) * heads_kv is below 2^27, and for the
+ * backward tokens_q * heads_q / heads_kv below 2^31 - 2^13.
  * Deterministic: the same inputs give the same bits on one GPU model.
  */
 typedef struct {

@@ -321,3 +321,13 @@ def test_attention_takes_a_million_sequences(L):
         a = ctypes.byref(_attn(batch=batch, **many))
         assert L.qlora_attention_fwd(a, None, None, None, None, None, None, 0, None) == want
         assert L.qlora_attention_bwd(a, *[None] * 10, 0, None) == want
+
+
+def test_attention_bwd_counts_rows_of_a_key_head_in_32_bits(L):
+    # the masks of a key are intervals of query rows (token * heads per key head): 2^31 of them do not fit
+    wide = dict(heads_q=64, heads_kv=1, head_dim=8, ld_q=512, ld_o=512, ld_k=8, ld_v=8, tokens_k=8)
+    most = ((1 << 31) - 1 - (128 << 6)) // 64
+    for tokens, want in ((most, 1), (most + 1, 2), (1 << 26, 2)):
+        a = ctypes.byref(_attn(tokens_q=tokens, **wide))
+        assert L.qlora_attention_bwd(a, *[None] * 10, 0, None) == want, tokens         # 1: the pointers, looked at after
+        assert L.qlora_attention_fwd(a, None, P[0], P[1], None, None, None, 0, None) == 1
