@@ -439,6 +439,17 @@ def _want(t, name: str, dtype, shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+_MOST = 2 ** 31 - 1
+
+
+def _i32(x, name: str) -> int:
+    """x for a 32-bit argument; ctypes alone would take its low bits."""
+    x = int(x)
+    if not -_MOST <= x <= _MOST:
+        raise ValueError(f"{name}: {x} does not fit 32 bits")
+    return x
+
+
 def _device(*tensors) -> int:
     """Index of the device that every given tensor lives on."""
     index = None
@@ -538,8 +549,9 @@ def qlora_rotary_init(head_dim: int, rot_dim: int | None = None, layout: str = "
     """Table of the pairs' turns per position: layout "half" or "interleaved"; scaling "none", "linear", "bands" or "yarn"."""
     if layout not in _ROTARY_LAYOUTS or scaling not in _ROTARY_SCALINGS:
         raise ValueError(f"unknown layout {layout!r} or scaling {scaling!r}")
-    cfg = RotaryConfig(int(head_dim), int(head_dim if rot_dim is None else rot_dim), _ROTARY_LAYOUTS[layout],
-                       _ROTARY_SCALINGS[scaling], base, factor, low, high, original_length, magnitude)
+    cfg = RotaryConfig(_i32(head_dim, "head_dim"), _i32(head_dim if rot_dim is None else rot_dim, "rot_dim"),
+                       _ROTARY_LAYOUTS[layout], _ROTARY_SCALINGS[scaling], base, factor, low, high, original_length,
+                       magnitude)
     rot = Rotary()
     _check(lib().qlora_rotary_init(ctypes.byref(cfg), ctypes.byref(rot)), "qlora_rotary_init")
     return rot
@@ -564,6 +576,8 @@ def qlora_rotary_apply(rot: Rotary, positions, q, q_out=None, k=None, k_out=None
     if k is not None:
         hk = k.shape[1]
         ldk, ldko = _head_rows(k, "k", (m, hk, d)), _head_rows(k_out, "k_out", (m, hk, d))
+    if hq > _MOST or hk > _MOST:
+        raise ValueError("more heads than fit 32 bits")
     _run("qlora_rotary_apply", _device(q, q_out, positions, k, k_out),
          (ctypes.byref(rot), at, m, q.data_ptr(), ldq, hq, q_out.data_ptr(), ldqo, _addr(k), ldk, hk,
           _addr(k_out), ldko, 1 if transpose else 0), stream)
@@ -574,6 +588,8 @@ def _residual(x):
     """(shape, type, its code) of the residual stream x [rows, cols]."""
     if x is None or x.dim() != 2:
         raise ValueError("the residual stream is [rows, cols], bf16 or fp32")
+    if x.shape[1] > _MOST:
+        raise ValueError(f"cols: {x.shape[1]} does not fit 32 bits")
     if x.dtype is torch.bfloat16:
         return x.shape, torch.bfloat16, QLORA_DTYPE_BF16
     if x.dtype is torch.float32:
@@ -595,7 +611,7 @@ def qlora_norm_residual_fwd(x, y, w_post, gate, w_pre, r, h, scale: float = 1.0,
 
 
 def qlora_norm_residual_workspace_bytes(rows: int, cols: int) -> int:
-    return int(lib().qlora_norm_residual_workspace_bytes(rows, cols))
+    return int(lib().qlora_norm_residual_workspace_bytes(rows, _i32(cols, "cols")))
 
 
 def qlora_norm_residual_bwd(dr, dh, r, y, w_post, gate, w_pre, dx, dy=None, dw_post=None, dgate=None, dw_pre=None,
@@ -610,7 +626,7 @@ def qlora_norm_residual_bwd(dr, dh, r, y, w_post, gate, w_pre, dx, dy=None, dw_p
             _dense(r, "r", res, shape), _dense(y, "y", bf, shape), _dense(w_post, "w_post", f32, vec),
             _dense(gate, "gate", f32, vec), _dense(w_pre, "w_pre", f32, vec), _dense(dx, "dx", res, shape),
             _dense(dy, "dy", bf, shape), _dense(dw_post, "dw_post", f32, vec), _dense(dgate, "dgate", f32, vec),
-            _dense(dw_pre, "dw_pre", f32, vec), int(flags))
+            _dense(dw_pre, "dw_pre", f32, vec), _i32(flags, "flags"))
     dev = _device(r, dr, dh, y, w_post, gate, w_pre, dx, dy, dw_post, dgate, dw_pre, ws)
     need = 0
     if ws is None and (dw_post is not None or dgate is not None or dw_pre is not None):
@@ -655,7 +671,9 @@ def _attention(Q, K, V, O, lse, batch, causal, window, scale, cu_q, cu_k) -> Att
         ld_k = ld_v = hk * d
     else:
         ld_q, ld_k, ld_v, ld_o = _heads(Q, "Q"), _heads(K, "K"), _heads(V, "V"), _heads(O, "O")
-    return Attention(1 if batch is None else int(batch), hq, hk, d, 1 if causal else 0, int(window),
+    if hq > _MOST or hk > _MOST or d > _MOST:
+        raise ValueError("more heads, or elements of one, than fit 32 bits")
+    return Attention(1 if batch is None else _i32(batch, "batch"), hq, hk, d, 1 if causal else 0, _i32(window, "window"),
                      d ** -0.5 if scale is None and d > 0 else float(scale or 0.0), 0, tq, tk, ld_q, ld_k, ld_v, ld_o,
                      at_q, at_k)
 
@@ -674,7 +692,7 @@ def qlora_attention_fwd(Q, K, V, O, lse=None, batch: int | None = None, causal: 
 
 
 def qlora_attention_bwd_workspace_bytes(tokens_q: int, heads_q: int) -> int:
-    return int(lib().qlora_attention_bwd_workspace_bytes(tokens_q, heads_q))
+    return int(lib().qlora_attention_bwd_workspace_bytes(tokens_q, _i32(heads_q, "heads_q")))
 
 
 def qlora_attention_bwd(Q, K, V, O, dO, lse, dQ, dK, dV, batch: int | None = None, causal: bool = False, window: int = 0,

@@ -331,3 +331,36 @@ def test_attention_bwd_counts_rows_of_a_key_head_in_32_bits(L):
         a = ctypes.byref(_attn(tokens_q=tokens, **wide))
         assert L.qlora_attention_bwd(a, *[None] * 10, 0, None) == want, tokens         # 1: the pointers, looked at after
         assert L.qlora_attention_fwd(a, None, P[0], P[1], None, None, None, 0, None) == 1
+
+
+def test_binding_refuses_what_does_not_fit_32_bits(L):
+    # the low 32 bits of each of these are a valid value
+    big, bf = 1 << 32, torch.bfloat16
+    meta = lambda *s, t=bf: torch.empty(*s, dtype=t, device="meta")  # noqa: E731
+    x = meta(4, 2, 64)
+    for kw in (dict(window=big, causal=True), dict(window=big + 5, causal=True), dict(window=5 - big, causal=True),
+               dict(batch=big + 1), dict(batch=1 - big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            q.qlora_attention_fwd(x, x, x, x, **kw)
+        with pytest.raises(ValueError, match="32 bits"):
+            q.qlora_attention_bwd(x, x, x, x, x, meta(4, 2, t=torch.float32), x, x, x, **kw)
+    for shape in ((1, 1, big + 64), (1, big + 2, 8)):
+        with pytest.raises(ValueError, match="32 bits"):
+            q.qlora_attention_fwd(*[meta(*shape)] * 4)
+    with pytest.raises(ValueError, match="32 bits"):
+        q.qlora_rotary_init(big + 64)
+    with pytest.raises(ValueError, match="32 bits"):
+        q.qlora_rotary_init(64, rot_dim=big + 64)
+    with pytest.raises(ValueError, match="32 bits"):
+        q.qlora_rotary_apply(q.qlora_rotary_init(8), meta(1, t=torch.int32), meta(1, big + 1, 8))
+    wide, vec = meta(1, big + 64), meta(big + 64, t=torch.float32)
+    with pytest.raises(ValueError, match="32 bits"):
+        q.qlora_norm_residual_fwd(wide, None, None, None, vec, None, wide)
+    with pytest.raises(ValueError, match="32 bits"):
+        q.qlora_norm_residual_bwd(None, wide, wide, None, None, None, vec, wide)
+    with pytest.raises(ValueError, match="32 bits"):
+        q.qlora_norm_residual_bwd(None, x[0], x[0], None, None, None, meta(64, t=torch.float32), x[0], flags=big)
+    with pytest.raises(ValueError, match="32 bits"):
+        q.qlora_norm_residual_workspace_bytes(4, big + 64)
+    with pytest.raises(ValueError, match="32 bits"):
+        q.qlora_attention_bwd_workspace_bytes(4, big + 2)
