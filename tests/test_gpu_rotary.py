@@ -130,3 +130,57 @@ def test_rotary_empty_and_other_stream():
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got, want)
     q.qlora_check_device_error()
+
+
+def heads_per_thread(m, hq, hk, d, rot, in_place):
+    """The run of heads that a thread takes, by the launch's rule."""
+    pairs = 8 if rot % 16 == 0 else 4
+    groups = rot // (2 * pairs) + (0 if in_place else -(-(d - rot) // 16))
+    blocks = -(-m // (256 // groups))
+    want = torch.cuda.get_device_properties(0).multi_processor_count // 3
+    run = 8
+    while run > 1 and blocks * (-(-hq // run) + -(-hk // run)) < want:
+        run //= 2
+    return run
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("d,rot", [(128, 128), (128, 64), (128, 40), (96, 80), (80, 24), (256, 128)])
+@pytest.mark.parametrize("m,hq,hk", [(2100, 28, 1), (2100, 13, 5), (2100, 32, 32), (2051, 9, 0)])
+def test_rotary_of_many_tokens(layout, d, rot, m, hq, hk):
+    # threads with runs of eight heads, in two batches of four: whole runs, runs of one to five heads, heads of q and of k
+    assert heads_per_thread(m, hq, hk, d, rot, False) == 8 == heads_per_thread(m, hq, hk, d, rot, True)
+    r = q.qlora_rotary_init(d, rot, layout, magnitude=0.8)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m + hq)
+    pos = torch.randint(-5, 1 << 17, (m,), generator=g, device="cuda", dtype=torch.int32)
+    # eight elements of other things between the tokens, which stay
+    wide = _bf(m, hq * d + 8, seed=4)
+    x = wide[:, :hq * d].view(m, hq, d)
+    k = _bf(m, hk, d, seed=1) if hk else None
+    for transpose in (False, True):
+        out = torch.full_like(wide, 3.0)
+        y, ky = out[:, :hq * d].view(m, hq, d), (None if k is None else torch.empty_like(k))
+        q.qlora_rotary_apply(r, pos, x, y, k, ky, transpose=transpose)
+        q.qlora_check_device_error()
+        assert (out[:, hq * d:] == 3).all()
+        for got, of in ((y, x), (ky, k)):
+            if of is not None:
+                _close(got, *_ref(r, pos, of, transpose))
+                assert torch.equal(got[..., rot:], of[..., rot:])
+        x2, k2 = wide.clone()[:, :hq * d].view(m, hq, d), (None if k is None else k.clone())
+        q.qlora_rotary_apply(r, pos, x2, k=k2, transpose=transpose)
+        assert torch.equal(x2, y) and (k is None or torch.equal(k2, ky))
+
+
+@pytest.mark.parametrize("m,hq,hk,run", [(150, 28, 1, 2), (260, 28, 1, 4), (40, 13, 5, 1)])
+def test_rotary_of_runs_in_between(m, hq, hk, run):
+    assert heads_per_thread(m, hq, hk, 128, 128, True) == run
+    r = q.qlora_rotary_init(128)
+    pos = torch.arange(m, device="cuda", dtype=torch.int32)
+    x, k = _bf(m, hq, 128), _bf(m, hk, 128, seed=1)
+    y, ky = torch.empty_like(x), torch.empty_like(k)
+    q.qlora_rotary_apply(r, pos, x, y, k, ky)
+    _close(y, *_ref(r, pos, x))
+    _close(ky, *_ref(r, pos, k))
+    q.qlora_check_device_error()
