@@ -491,6 +491,11 @@ int qlora_norm_residual_bwd(const qlora_norm *n, const void *dr, const uint16_t 
  *    offsets; any lengths, zero included; values outside the tensors are clamped).
  *    Both NULL: batch sequences of equal length. Tokens in no sequence are not
  *    read as queries, and their rows of O, lse and the gradients stay as they were.
+ *    A cache of `slots` places for `capacity` keys each, of which the first len[s]
+ *    are filled: the room behind them is a sequence without queries, so batch =
+ *    2 slots, cu_k[2 s] = s capacity, cu_k[2 s + 1] = s capacity + len[s], and
+ *    cu_q[2 s + 1] = cu_q[2 s + 2], slot s's new queries being cu_q[2 s] onwards.
+ *    The room may hold anything.
  *  - causal: query i of nq sees key j of nk iff j <= i + nk - nq (the last query
  *    sees all keys: nq < nk continues a sequence whose earlier keys are kept).
  *    window > 0 (causal only): of those, the last `window` keys. A query that

@@ -626,3 +626,33 @@ def test_a_tile_that_takes_seconds():
         c = d ** -0.5
         assert ((dQ[at].double() - c * want).abs() <= H * c * want.abs() + (H + F) * c * size).all()
     assert not dQ[:nq - 3].any()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (4, 4, 64)])
+@pytest.mark.parametrize("new", [1, 3])
+def test_a_cache_with_room_behind_its_keys(hq, hkv, d, new):
+    # the layout that the header names: every slot two sequences, its keys and the room behind them, which holds NaN
+    slots, capacity = 5, 700
+    lens = [300, 3, 700, 64, 129]
+    p = Problem([x for _ in range(slots) for x in (new, 0)], [x for n in lens for x in (n, capacity - n)], hq, hkv, d, True,
+                seed=21)
+    for s, n in enumerate(lens):
+        for t in (p.K, p.V):
+            t[s * capacity + n:(s + 1) * capacity] = float("nan")
+    check(p)
+    if new == 1:        # the offsets as the README makes them
+        starts = torch.arange(slots, device="cuda") * capacity
+        cu_k = torch.stack((starts, starts + torch.tensor(lens, device="cuda")), 1).flatten()
+        cu_k = torch.cat((cu_k, cu_k.new_tensor([slots * capacity]))).int()
+        cu_q = (torch.arange(2 * slots + 1, device="cuda") + 1).div(2, rounding_mode="floor").int()
+        assert torch.equal(cu_q, p.cu_q) and torch.equal(cu_k, p.cu_k)
+
+
+@pytest.mark.parametrize("q_lens,k_lens,hq,hkv,d,window", [
+    ([1] * 63 + [2048], [100 + 40 * i for i in range(63)] + [2048], 4, 4, 64, 0),     # a prompt among single new tokens
+    ([2048] + [1] * 63, [2500] + [700] * 63, 8, 2, 128, 300),
+    ([1, 5] * 8, [900] * 16, 8, 2, 128, 0),                                           # one and five new tokens in turn
+    ([2] * 20 + [1000] + [0] * 30, [64] * 20 + [1000] + [5] * 30, 2, 1, 64, 0),
+])
+def test_prompts_among_new_tokens(q_lens, k_lens, hq, hkv, d, window):
+    check(Problem(q_lens, k_lens, hq, hkv, d, True, window, seed=len(q_lens)))
