@@ -236,3 +236,26 @@ def test_norm_captured_and_replayed_on_another_stream():
 def test_norm_many_rows(m, cols, kind, dt):
     # several rows for every group of threads, in rings of one to four rows
     test_norm_forward_and_backward(m, cols, kind, dt)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,cols", [(2100, 4096), (950, 8192), (500, 16384)])
+def test_norm_many_rows_in_place(m, cols, dt):
+    # r over x, h over y, dx over dr and dy over dh, while the next rows are on their way; and what may be left out
+    c = Case(m, cols, True, True, True, True, dt, seed=cols)
+    r, h = _run_fwd(c)
+    x, y = c.x.clone(), c.y.clone()
+    q.qlora_norm_residual_fwd(x, y, *c.vectors(), x, y, scale=SCALE, eps=EPS)
+    assert torch.equal(x, r) and torch.equal(y, h)
+    for weights in (True, False):
+        got = _run_bwd(c, r, c.dr, weights)
+        dr, dh = c.dr.clone(), c.dh.clone()
+        dw = [torch.empty_like(t) if weights else None for t in c.vectors()]
+        q.qlora_norm_residual_bwd(dr, dh, r, c.y, *c.vectors(), dr, dh, *dw, scale=SCALE, eps=EPS)
+        assert torch.equal(dr, got["dx"]) and torch.equal(dh, got["dy"])
+        assert not weights or all(torch.equal(a, got[n]) for a, n in zip(dw, ("dw_post", "dgate", "dw_pre")))
+        # no dy, and one weight gradient of three
+        dx, dg = torch.empty_like(r), torch.empty_like(c.gate) if weights else None
+        q.qlora_norm_residual_bwd(c.dr, c.dh, r, c.y, *c.vectors(), dx, None, None, dg, scale=SCALE, eps=EPS)
+        assert torch.equal(dx, got["dx"]) and (not weights or torch.equal(dg, got["dgate"]))
+    q.qlora_check_device_error()
