@@ -23,9 +23,10 @@
 // 16 warps work on alternate halves of a step: keys: dV of a step and S of the next while dS is
 // formed, dK and the next dP while the next S is exponentiated; queries: S is two steps ahead
 // (two buffers; dS goes back over S, so that dP's columns are free as soon as they are read).
-// Measured (heads of 128): 4 x 2048 tokens, 64 heads, causal 980 to 1080 us; 8192 tokens, 16 heads, causal 809 us, not
-// causal 1438 (1338 TFLOP/s of the 7 products). Tensor pipe 54 to 57% busy, issue 47%: the 16 warps' two phases of a step
-// wait for one another's products.
+// Measured (heads of 128): 4 x 2048 tokens, 64 heads, causal 990 us a call by itself at 1.97 GHz, 1169 back to back for a
+// second, where the power cap leaves 1.52. Back to back, 8192 tokens, 16 heads: causal 941 us (1.57 GHz), not causal 1681
+// (1.49 GHz; 1145 TFLOP/s of the 7 products). Tensor pipe 54 to 57% busy, issue 47%: the 16 warps' two phases of a step wait
+// for one another's products. The keys' kernel spills 12 bytes at its 96 registers.
 // Blocks are persistent, so that a tile's loads and first products run under the end of the tile
 // before. (As a block per tile, 16,000 of a tile's 47,000 cycles were its beginning and its end.)
 #include <algorithm>
@@ -40,8 +41,8 @@ namespace {
 
 constexpr int kStep = 128;            // streamed rows per step
 constexpr int kMathWarps = 16;
-// Of four exponentials, those by polynomial (4 causal sequences of 2048 tokens, 64 heads of 128: 983 us with none, 975 with
-// one, 998 with two, 1010 with three; 8192 tokens of 32 heads: 1753, 1700, 1798).
+// Of four exponentials, those by polynomial (back to back, 4 causal sequences of 2048 tokens, 64 heads of 128: 1175 us with
+// none, 1169 with one, 1196 with two, 1244 with three; 8192 tokens of 32 heads: 1864, 1829, 1895, 1971).
 constexpr int kPolyOf4 = 1;
 constexpr int kBwdThreads = (kMathWarps + 4) * 32;
 
@@ -680,8 +681,9 @@ cudaError_t launch(AttnParams p, const AttnMaps& maps, int num_sms, cudaStream_t
   const int64_t tiles = (kKeys ? p.cu_k : p.cu_q) == nullptr ? p.batch * ((tokens / p.batch + per - 1) / per)
                                                              : std::min<int64_t>(tokens, tokens / per + p.batch);
   p.tiles = static_cast<int32_t>(tiles);
-  // heads walked together: those whose streamed tensors (of a mean sequence) share a quarter of the L2 cache (8192 tokens, 64
-  // heads: 3576 us, one at a time 3625; 4 x 2048: 1170, one 1180, all 1277)
+  // heads walked together: those whose streamed tensors (of a mean sequence) share a quarter of the L2 cache (back to
+  // back, 8192 tokens, 64 heads: 3609 us, one at a time 3667, all 4076; 32 heads: 1829, 1871, 1901; 4 x 2048, 64 heads: 1169,
+  // 1177, 1184)
   const int64_t bytes = std::max<int64_t>(1, (kKeys ? p.tokens_q * p.group : p.tokens_k) / p.batch) * p.head_dim * 4;
   p.head_run = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(p.heads_kv, (int64_t(32) << 20) / bytes)));
   const int64_t blocks = tiles * p.heads_kv;

@@ -11,12 +11,13 @@
 // and a second kernel, which starts under the end of the first, joins them in a fixed order: no
 // atomics, the same bits on every call.
 //
-// Measured (8 key heads of 128, 4 query heads each, one query a sequence; keys and values at the
-// copy's rate would take): 16 ragged sequences of 28,900 keys 28.4 us (18.0), 16 of 4096 49.5 (40.9),
-// 16 of 8192 89 (81.7), 19 of 1811 32 (21.5), one of 16384 20 (10.2). Of a call 6 us are its
-// beginning and end (finding the run 1, first loads 1.5), 2 to 3 the second kernel. A cluster of
-// blocks per tile that joined its results in shared memory took 34.5, 50, 89, 54 and 22 us: blocks of
-// unequal length, a second round of them (4 us), and 4 us to join.
+// Measured back to back (8 key heads of 128, 4 query heads each, one query a sequence; keys and values
+// at the copy's rate would take): 16 ragged sequences of 28,900 keys 29.3 us (18.0), 16 of 4096 51.0
+// (40.9), 16 of 8192 92.5 (81.7), 19 of 1811 32.9 (21.5), one of 16384 20.1 (10.2). Of a call 6 us are
+// its beginning and end (finding the run 1, first loads 1.5), 2 to 3 the second kernel. A cluster of
+// blocks per tile that joined its results in shared memory took 34.5, 50, 89, 54 and 22 us in a run in
+// which this form took 28.4, 49.5, 89, 32 and 20: blocks of unequal length, a second round of them (4
+// us), and 4 us to join.
 //
 // A block: 4 warps softmax, 1 warp MMAs, 1 warp that finds the segments of the run and feeds Q, and K
 // and V through a ring each, by TMA. Loads and first products of a segment run under the end of the
@@ -31,9 +32,12 @@ namespace qlora {
 namespace {
 
 constexpr int kStep = kFwdStep;
-// What a tile's beginning and end cost, in steps (the ragged sequences above: 37 us with 0, 29.8 with 1, 28.4 with 3).
+// What a tile's beginning and end cost, in steps. Back to back, the ragged sequences above: 38.3 us with 0, 31.1 with 1, 30.6
+// with 2, 30.1 with 3, 30.5 with 5; 300 sequences of 130 to 1200 keys: 192.7, 167.8, 157.6, 154.6, 153.9. Equal sequences,
+// whose runs cut them alike, move by 7% at most.
 constexpr int kSwitch = 3;
-// Tiles of so many steps stay whole (16 sequences of 256 keys: 11.6 us, cut 12.8), and all tiles where none can have
+// Tiles of so many steps stay whole (16 sequences of 256 keys: 11.5 us, from 2 steps on cut 13.0; 300 of 130 to 1200: 154.6 and
+// 152.9), and all tiles where none can have
 // more than kAllWhole: the second launch and its workspace cost a caller 5 us. Others are not cut closer than kSnap steps
 // to their ends.
 constexpr int kWhole = 4, kAllWhole = 16, kSnap = 2;

@@ -18,8 +18,9 @@
 // The output accumulates in tensor memory and is rescaled there, which few tiles ever ask for.
 //
 // Bound by the exponentials and the products in turns: a step of 2100 cycles holds 1050 of each (exp unit 52% busy, tensor
-// pipe 51%). 64 heads of 128, causal: 2 x 4096 tokens 535 us (1030 TFLOP/s); 16 heads: 8192 tokens 244 us (1128),
-// not causal 490 (1120).
+// pipe 51%). 64 heads of 128, causal, 2 x 4096 tokens: 541 us (1017 TFLOP/s) a call by itself at 1.97 GHz, 623 (882) back to
+// back for a second, where the power cap leaves 1.63. 16 heads, 8192 tokens, back to back: 285 us (965 TFLOP/s, 1.65 GHz), not
+// causal 566 (971, 1.72).
 #include <algorithm>
 #include <climits>
 #include <cstring>
@@ -354,7 +355,7 @@ cudaError_t launch_attn_fwd(AttnParams p, const uint16_t* Q, const uint16_t* K, 
   if (few) return launch_attn_few(p, maps, static_cast<float*>(ws), st);
   p.tiles = static_cast<int32_t>(attn_tiles(p, 2 * most));
   // heads walked together: those whose keys and values (of a mean sequence) share a quarter of the L2 cache (2 x 4096 tokens,
-  // 64 heads: 520 us; one head at a time 541, all 547)
+  // 64 heads, in turns in one run: 520 us; one head at a time 541, all 547)
   const int64_t kv = std::max<int64_t>(1, p.tokens_k / p.batch) * p.head_dim * 4;
   p.head_run = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(p.heads_kv, (int64_t(32) << 20) / kv)));
   const int64_t blocks = static_cast<int64_t>(p.tiles) * p.heads_kv;

@@ -15,8 +15,8 @@
 // the unrounded r. The backward recomputes eta and rho from the r and y it reads anyway, so
 // nothing but r and y is kept between the two directions.
 //
-// Bound by HBM: 8 bytes per element forward (bf16 stream), 12 backward (8192 x 8192: 92 us, 5.8 TB/s, and 160 us with
-// all weight gradients, 5.0 TB/s). Many rows: persistent
+// Bound by HBM: 8 bytes per element forward (bf16 stream), 12 backward (8192 x 8192, back to back: 91 us, 5.9 TB/s, and
+// 158 us with all weight gradients, 5.1 TB/s). Many rows: persistent
 // blocks, whose rows arrive by bulk copies into a ring of shared memory, so that the next rows'
 // loads run while a row's sums make the block wait; the weight vectors sit in shared memory too
 // (read from L2 for every row, they cost the backward half its time). Few rows: a block per row.
@@ -613,8 +613,11 @@ int grads_vec(int cols) { return cols <= 4096 ? 1 : cols <= 8192 ? 2 : 4; }
 int threads_of(int cols, int vec) { return round32((cols / 8 + vec - 1) / vec); }
 
 // A block of the persistent kernels: `groups` groups of `threads` threads, each with a ring of `stages` rows, `per_sm`
-// blocks on an SM; the weight vectors in shared memory if they leave every group two rows, or if without them no more
-// would fit.
+// blocks on an SM; the weight vectors in shared memory if they leave every group two rows, or one where there are several
+// groups or where without them no more would fit. The rule was measured on the bf16 stream. An fp32 stream's rows are longer
+// and it serves them less well: of the copy's rate, 8192 rows back to back, 2048 and 4096 columns 85 and 87% with one frozen
+// norm and 61 and 65% with both norms' gradients; 8192 columns, whose weights it leaves in L2, 96% with the pre-norm's
+// gradient, 64 with both norms', and 67 and 46% frozen (one norm, both), where a block has one group of 8 warps.
 constexpr size_t kSmemMost = 232448;
 constexpr size_t smem_static(int groups) { return 512 + static_cast<size_t>(groups > 1 ? kMaxGroups : 1) * 1088; }
 struct RingPlan {
@@ -699,7 +702,7 @@ cudaError_t launch_norm_bwd(const NormParams& p, bool f32, int num_sms, cudaStre
   const size_t stage = static_cast<size_t>(p.cols) *
                        (res + (p.dr != nullptr ? res : 0) + (p.dh != nullptr ? 2 : 0) + (p.y != nullptr ? 2 : 0));
   if (p.part == nullptr) {
-    // frozen: two vectors per thread, as many groups as 768 threads hold (4096 x 4096: 35 us, with one vector 44), four
+    // frozen: two vectors per thread, as many groups as 768 threads hold (4096 x 4096, bf16: 35 us, with one vector 44), four
     // above 6144 columns, where two would leave room for one group. Few rows: one vector, as with weight gradients up to
     // 4096 columns, whose sums are then in the same order (16 x 4096: 3.4 us either way, 296 x 4096 4.9 and 4.5).
     const int vec = p.rows <= 2 * num_sms && p.cols <= 6144 ? 1 : p.cols <= 6144 ? 2 : 4;
